@@ -91,10 +91,9 @@ __device__ __forceinline__ WarpPlace place(int64_t x, int kc_count) {
 }
 
 template <int ELT, bool NV>
-__global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const void* __restrict__ src, int64_t ld,
-                                                                 int64_t rows, int64_t cols, int kc_count,
-                                                                 NvScale sc, uint8_t* __restrict__ q,
-                                                                 uint8_t* __restrict__ s) {
+__global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const void* src, int64_t ld, int64_t rows,
+                                                                 int64_t cols, int kc_count, NvScale sc, uint8_t* q,
+                                                                 uint8_t* s) {
   constexpr int kLanes = NV ? 8 : 16, kBlock = NV ? 2 : 4;  // lanes per quad, per block
   constexpr int kWidth = 8 * kLanes;                        // columns of a quad
   __shared__ float2 tab[NV ? 128 : 1];
@@ -153,23 +152,22 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const void* __r
 }
 
 template <int ELT, bool NV>
-__global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t* __restrict__ q,
-                                                                   const uint8_t* __restrict__ s, int64_t rows,
-                                                                   int64_t cols, int kc_count, float ts,
-                                                                   void* __restrict__ dst, int64_t ld) {
+__global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t* q, const uint8_t* s, int64_t rows,
+                                                                   int64_t cols, int kc_count, float ts, void* dst,
+                                                                   int64_t ld) {
   constexpr int kBlock = NV ? 2 : 4;
   const WarpPlace p = place<NV>(blockIdx.x, kc_count);
   const int lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
   if (p.col >= cols) return;
-  const uint4 lv = __ldg(reinterpret_cast<const uint4*>(s + p.chunk));
+  const uint4 lv = *reinterpret_cast<const uint4*>(s + p.chunk);
   const uint32_t line[4] = {lv.x, lv.y, lv.z, lv.w};
   uint32_t codes[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     codes[i] = p.row0 + 32 * i < rows
-                   ? __ldg(reinterpret_cast<const uint32_t*>(q + (p.row0 + 32 * i) * (cols / 2) + p.col / 2))
+                   ? *reinterpret_cast<const uint32_t*>(q + (p.row0 + 32 * i) * (cols / 2) + p.col / 2)
                    : 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -27,7 +27,11 @@ inline NvScale nv_scale(float ts) {
   return NvScale{ts, ts6, static_cast<float>(1.0 / static_cast<double>(ts6))};
 }
 
-// Eight consecutive values of a row, as loaded.
+// Eight consecutive values of a row, as loaded. With ordinary loads: a kernel
+// here is resident while its predecessor may still write them (it waits before
+// it reads), and the read-only path (ld.global.nc, which `const __restrict__`
+// invites too) is for memory that nothing writes during the kernel's lifetime;
+// such loads may be moved above the wait.
 template <int ELT>
 struct Raw8 {
   uint32_t w[ELT == MOE_ELT_FP32 ? 8 : 4];
@@ -38,11 +42,11 @@ __device__ __forceinline__ Raw8<ELT> load_raw8(const void* base, int64_t at) {
   Raw8<ELT> r;
   if constexpr (ELT == MOE_ELT_FP32) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
-    const uint4 a = __ldg(p), b = __ldg(p + 1);
+    const uint4 a = p[0], b = p[1];
     r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
     r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
     r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
   }
   return r;
