@@ -224,6 +224,14 @@ def mxfp8_weights(operands: dict) -> MXFP8Weights:
     return st
 
 
+def stream_scope(stream):
+    """Context in which torch works and allocates on `stream` (a Stream or a raw
+    handle; None: the current one), as the library does when it is given it."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)  # None changes nothing
+
+
 def weights(wg, wu, wd, wg_bwd=None, wu_bwd=None, wd_bwd=None, mx: MXFP8Weights = None) -> Weights:
     w = Weights(_ptr(wg), _ptr(wu), _ptr(wd), _ptr(wg_bwd), _ptr(wu_bwd), _ptr(wd_bwd),
                 ctypes.pointer(mx) if mx is not None else None)

@@ -48,13 +48,16 @@ class FP4Tensor:
     def of_weight(cls, w, format="nvfp4", stream=None) -> "FP4Tensor":
         """w [rows, cols] quantised, for NVFP4 with the power of two as tensor scale
         that puts the largest magnitude at the top of both levels (6 * 448) or
-        just below: reads that magnitude on the host, so call it at load time."""
-        scale = 1.0
-        if _format(format) == _lib.FP4_NV:
-            top = float(w.abs().max()) if w.numel() else 0.0
-            if 0.0 < top < math.inf:
-                scale = 2.0 ** min(60, max(-60, math.ceil(math.log2(top / (6.0 * 448.0)))))
-        return cls(*w.shape, format=format, scale=scale, device=w.device).quantize(w, stream)
+        just below: reads that magnitude on the host, so call it at load time.
+        Everything runs on `stream`, and the result's memory belongs to it, as that
+        of a tensor made under torch.cuda.stream(stream)."""
+        with _lib.stream_scope(stream):
+            scale = 1.0
+            if _format(format) == _lib.FP4_NV:
+                top = float(w.abs().max()) if w.numel() else 0.0
+                if 0.0 < top < math.inf:
+                    scale = 2.0 ** min(60, max(-60, math.ceil(math.log2(top / (6.0 * 448.0)))))
+            return cls(*w.shape, format=format, scale=scale, device=w.device).quantize(w)
 
     def on_device(self):
         """Raises unless the buffers are on the GPU (kernels would fault on host addresses)."""
@@ -71,9 +74,11 @@ class FP4Tensor:
         return self
 
     def dequantize(self, out=None, dtype=torch.bfloat16, stream=None):
-        """The values the codes stand for, rounded once to out's type."""
+        """The values the codes stand for, rounded once to out's type. Without out, the
+        memory is taken on `stream` (as under torch.cuda.stream(stream))."""
         if out is None:
-            out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.q.device)
+            with _lib.stream_scope(stream):
+                out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.q.device)
         elt = _elt(out)
         op, ld = matrix_ptr("out", out, self._shape, out.dtype)
         self.on_device()
