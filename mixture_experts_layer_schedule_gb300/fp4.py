@@ -31,18 +31,56 @@ def _elt(t):
 class FP4Tensor:
     """A [rows, cols] matrix in 4 bits (cols a multiple of 32): packed codes q,
     block scales s in the order the products read, and the tensor scale (NVFP4;
-    1 for MXFP4) that quantize() and every reader apply."""
+    1 for MXFP4) that quantize() and every reader apply. All three may be set, to
+    another scale or to stored codes and scales of the same sizes; every later
+    call uses them."""
 
     def __init__(self, rows, cols, format="nvfp4", scale=1.0, device="cuda"):
         self.rows, self.cols, self.format = int(rows), int(cols), _format(format)
-        self.scale = float(scale)
         n = _lib.fp4_scale_bytes(self.format, rows, cols)  # also checks the sizes
         dev = torch.device(device)
-        self.q = torch.empty((self.rows, self.cols // 2), dtype=torch.uint8, device=dev)
-        self.s = torch.empty(n, dtype=torch.uint8, device=dev)
-        self.operand = _lib.FP4Operand(self.q.data_ptr(), self.s.data_ptr(), self.scale)
+        self._q = torch.empty((self.rows, self.cols // 2), dtype=torch.uint8, device=dev)
+        self._s = torch.empty(n, dtype=torch.uint8, device=dev)
+        # what the library is handed; the setters below keep it in step
+        self.operand = _lib.FP4Operand(self._q.data_ptr(), self._s.data_ptr(), 1.0)
+        self.scale = scale
         self._shape, self._operand = (self.rows, self.cols), ctypes.byref(self.operand)
-        self._cuda = self.q.is_cuda
+        self._cuda = self._q.is_cuda
+
+    @property
+    def scale(self) -> float:
+        return self._scale
+
+    @scale.setter
+    def scale(self, value):
+        self._scale = self.operand.scale = float(value)
+
+    @property
+    def q(self) -> torch.Tensor:
+        return self._q
+
+    @q.setter
+    def q(self, t):
+        self.operand.q = self._buffer("q", t, self._q)
+        self._q = t
+
+    @property
+    def s(self) -> torch.Tensor:
+        return self._s
+
+    @s.setter
+    def s(self, t):
+        self.operand.s = self._buffer("s", t, self._s)
+        self._s = t
+
+    @staticmethod
+    def _buffer(name, t, old):
+        if t.device != old.device:
+            raise ValueError(f"{name}: expected a tensor on {old.device}, got one on {t.device}")
+        if t.shape != old.shape or t.dtype != old.dtype or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {old.dtype} of shape {tuple(old.shape)}, got {t.dtype} "
+                             f"of shape {tuple(t.shape)}")
+        return t.data_ptr()
 
     @classmethod
     def of_weight(cls, w, format="nvfp4", stream=None) -> "FP4Tensor":
