@@ -159,7 +159,8 @@ __device__ __forceinline__ uint32_t quantize8(const Raw8<ELT>& raw, const NvScal
     const float inv = __uint_as_float(static_cast<uint32_t>(254 - code) << 23);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] *= inv;
-    codes = biased > 0 && !bad ? e2m1x8(f) : 0u;
+    // a subnormal amax too: its products with 2^127 are exact
+    codes = top > 0 && !bad ? e2m1x8(f) : 0u;
     return bad ? kNanE8m0 : static_cast<uint32_t>(code);
   }
 }
