@@ -180,11 +180,18 @@ class FP4Linear:
 class FP4GatedFFN:
     """The gated feed-forward block of GatedFFN with 4-bit weights, for serving:
     the gated product, then the down product, each quantising its input in the
-    call. Two launches for up to 32 tokens."""
+    call. Two launches for up to 32 tokens.
 
-    def __init__(self, N, H, I, format="nvfp4", dtype=torch.bfloat16, activation="silu", device="cuda"):
-        self.gate_up = FP4Linear(N, I, H, format=format, dtype=dtype, activation=activation, device=device)
-        self.down = FP4Linear(N, H, I, format=format, dtype=dtype, device=device)
+    x_scale and act_scale are the NVFP4 tensor scales of x and of the inner
+    activations. At 1 a block of 16 values whose largest magnitude is at most
+    6 * 2^-10 becomes zeros, and below 6 * 2^-6 its scale keeps three bits or fewer;
+    a power of two near max|x| / (6 * 448) uses the format's whole range."""
+
+    def __init__(self, N, H, I, format="nvfp4", dtype=torch.bfloat16, activation="silu", device="cuda",
+                 x_scale=1.0, act_scale=1.0):
+        self.gate_up = FP4Linear(N, I, H, format=format, dtype=dtype, activation=activation, x_scale=x_scale,
+                                 device=device)
+        self.down = FP4Linear(N, H, I, format=format, dtype=dtype, x_scale=act_scale, device=device)
 
     @staticmethod
     def quantize_weights(wg, wu, wd, format="nvfp4"):
