@@ -203,3 +203,7 @@ class FP4GatedFFN:
 
     def device_error(self, stream=None) -> int:
         return self.gate_up.device_error(stream) or self.down.device_error(stream)
+
+    def clear_device_error(self, stream=None):
+        self.gate_up.clear_device_error(stream)
+        self.down.clear_device_error(stream)

@@ -46,3 +46,13 @@ def test_mxfp4_has_no_tensor_scale():
     for kw in (dict(x_scale=2.0), dict(act_scale=0.5)):
         with pytest.raises(MoEError):
             FP4GatedFFN(4, 64, 64, format="mxfp4", **kw).forward(x, *q)
+
+
+def test_error_words_can_be_cleared():
+    """Both products' error words, set here on the host's behalf, read as zero again."""
+    f = FP4GatedFFN(4, 64, 64)
+    for product in (f.gate_up, f.down):
+        product.ws[:4].view(torch.int32).fill_(3)
+        assert f.device_error() == 3
+        f.clear_device_error()
+        assert f.device_error() == 0 and product.device_error() == 0
