@@ -788,6 +788,9 @@ __global__ void __launch_bounds__(kSplitThreads)
     constexpr uint32_t kWStep = (kSplitMn<MODE> ? 2048 : 32) >> 4;
     const uint32_t w_lo0 = sdesc_lo(smem_u32(smem), kSplitMn<MODE> ? kHalfTile / 2 : 16);
     const uint32_t x_lo0 = sdesc_lo(smem_u32(smem + kHalfTile), 16);
+    // Every role waits for the previous kernel before its first barrier: the
+    // barriers' limit must not run while that kernel does.
+    grid_dep_wait();
     for (int i = 0; i < n_mine; ++i) {
       const int s = i % C::stages;
       if (!warp_wait(&full_bar[s], (i / C::stages) & 1, abortp, args.err)) break;

@@ -642,6 +642,9 @@ __global__ void __launch_bounds__(kSplitThreads) fp4_split_kernel(const __grid_c
     // column of the tile's first token in its 128-row scale chunk (QX: always 0)
     const uint32_t sfx_quarter = QX ? 0u : (tok0 % 128) / 32;
     const uint32_t lo0 = sdesc_lo(smem_u32(smem), 16);
+    // As every role: the previous kernel first, so that the barriers' limit does
+    // not run while that kernel does.
+    grid_dep_wait();
     for (int i = 0; i < n_mine; ++i) {
       const int s = i % C::stages;
       if (!warp_wait(&full_bar[s], (i / C::stages) & 1, abortp, args.err)) break;
