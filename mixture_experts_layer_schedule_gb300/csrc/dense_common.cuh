@@ -8,7 +8,9 @@
 
 #include <algorithm>
 
+#include "context_cache.h"
 #include "moe_common.cuh"
+#include "moe_internal.h"
 #include "tma_map.h"
 
 namespace moe {
@@ -323,6 +325,15 @@ inline int device_sms() {
     return n > 0 ? n : 148;
   }();
   return sms;
+}
+
+// Raises a kernel's dynamic shared-memory limit, which holds in the current
+// context only. A refusal is left to the caller, not to the next launch's check.
+template <class K>
+bool set_smem(K kernel, int bytes) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
+  (void)cudaGetLastError();
+  return false;
 }
 
 // Microseconds of a split kernel's parts, fitted to a GB300 over 20 to 40 problem

@@ -32,10 +32,8 @@
 // Loads past an edge read zeros and stores past it are dropped, so N is any
 // number >= 0 and H, I any multiples of 8 (16-byte row pitch).
 #include <algorithm>
-#include <mutex>
 
 #include "dense_common.cuh"
-#include "moe_internal.h"
 
 namespace moe {
 namespace {
@@ -838,25 +836,28 @@ __global__ void __launch_bounds__(kSplitThreads)
 // ---------------------------------------------------------------------------
 // Host side.
 
-template <class K>
-bool set_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
+// Co-resident clusters of 1 to 4 CTA pairs of the pair kernel.
+struct PairClusters {
+  int n[5];
+};
 
-// Co-resident clusters of `pairs` CTA pairs of the pair kernel on this device.
+// Those of `pairs` pairs on the current device; 0 if it cannot be told.
 template <int MODE, bool KSPLIT>
 int pair_clusters(int pairs) {
-  static std::once_flag once;
-  static int n[5] = {};
-  std::call_once(once, [] {
-    if (!set_smem(dense_pair_kernel<MODE, KSPLIT>, PCfg<MODE>::smem)) return;
+  static ContextCache<PairClusters> cache;
+  PairClusters v{};
+  const bool ok = cache.get(current_context_id, [](PairClusters& c) {
+    if (!set_smem(dense_pair_kernel<MODE, KSPLIT>, PCfg<MODE>::smem)) return false;
     for (int p = 1; p <= (KSPLIT ? 4 : 1); ++p) {
-      LaunchCfg c(dim3(2 * p), kThreads, PCfg<MODE>::smem, 2 * p, false, nullptr);
-      int m = 0;
-      if (cudaOccupancyMaxActiveClusters(&m, dense_pair_kernel<MODE, KSPLIT>, &c.cfg) == cudaSuccess) n[p] = m;
+      LaunchCfg l(dim3(2 * p), kThreads, PCfg<MODE>::smem, 2 * p, false, nullptr);
+      if (cudaOccupancyMaxActiveClusters(&c.n[p], dense_pair_kernel<MODE, KSPLIT>, &l.cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+      }
     }
-  });
-  return n[pairs];
+    return true;
+  }, v);
+  return ok ? v.n[pairs] : 0;
 }
 
 template <int MODE>
@@ -893,10 +894,10 @@ moe_status launch_wgrad(const DMaps& m, DArgs a, cudaStream_t s) {
 
 template <int MODE, int NT>
 moe_status launch_split_nt(const SMaps& m, const DArgs& a, int w_tiles, cudaStream_t s) {
-  static std::once_flag once;
-  static bool ok = false;
-  std::call_once(once, [] { ok = set_smem(dense_split_kernel<MODE, NT>, SplitCfg<NT>::smem); });
-  if (!ok) return MOE_ERR_CUDA;
+  static ContextCache<bool> cache;
+  bool raised;
+  if (!cache.get(current_context_id, [](bool& v) { return v = set_smem(dense_split_kernel<MODE, NT>, SplitCfg<NT>::smem); }, raised))
+    return MOE_ERR_CUDA;
   LaunchCfg c(dim3(static_cast<unsigned>(w_tiles * a.t_tiles * a.splits)), kSplitThreads, SplitCfg<NT>::smem, a.splits, true, s);
   if (cudaLaunchKernelEx(&c.cfg, dense_split_kernel<MODE, NT>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
   note_launch();

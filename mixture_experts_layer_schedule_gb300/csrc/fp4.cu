@@ -30,7 +30,6 @@
 
 #include "dense_common.cuh"
 #include "fp4.cuh"
-#include "moe_internal.h"
 
 namespace moe {
 namespace {

@@ -34,11 +34,9 @@
 //    through 4096 x 1536 (3.5 MB) in 3.2 us, gated 1536, K = 4096 (7.1 MB) in
 //    4.1 us; 64 tokens through 7168 x 2048 in 6 us.
 #include <algorithm>
-#include <mutex>
 
 #include "dense_common.cuh"
 #include "fp4.cuh"
-#include "moe_internal.h"
 
 namespace moe {
 namespace {
@@ -734,23 +732,19 @@ __global__ void __launch_bounds__(kSplitThreads) fp4_split_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // Host side.
 
-template <class K>
-bool set_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
 template <bool NV, bool GATED>
 moe_status launch_pair(const FMaps& m, const FArgs& a, cudaStream_t s) {
   using C = F4Pair<GATED>;
-  static std::once_flag once;
-  static int most = 0;
-  std::call_once(once, [] {
-    if (!set_smem(fp4_pair_kernel<NV, GATED>, C::smem)) return;
+  static ContextCache<int> cache;
+  int most = 0;  // co-resident pairs on the current device
+  const bool ok = cache.get(current_context_id, [](int& n) {
+    if (!set_smem(fp4_pair_kernel<NV, GATED>, C::smem)) return false;
     LaunchCfg c(dim3(2), C::threads, C::smem, 2, false, nullptr);
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp4_pair_kernel<NV, GATED>, &c.cfg) == cudaSuccess) most = n;
-  });
-  if (most <= 0) return MOE_ERR_CUDA;
+    if (cudaOccupancyMaxActiveClusters(&n, fp4_pair_kernel<NV, GATED>, &c.cfg) == cudaSuccess) return true;
+    (void)cudaGetLastError();
+    return false;
+  }, most);
+  if (!ok || most <= 0) return MOE_ERR_CUDA;
   LaunchCfg c(dim3(2 * static_cast<unsigned>(std::min<int64_t>(most, a.tiles))), C::threads, C::smem, 2, true, s);
   if (cudaLaunchKernelEx(&c.cfg, fp4_pair_kernel<NV, GATED>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
   note_launch();
@@ -760,10 +754,10 @@ moe_status launch_pair(const FMaps& m, const FArgs& a, cudaStream_t s) {
 template <bool NV, bool GATED, int NT, bool QX>
 moe_status launch_split_nt(const FMaps& m, FArgs a, int w_tiles, cudaStream_t s) {
   using C = F4Split<GATED, NT>;
-  static std::once_flag once;
-  static bool ok = false;
-  std::call_once(once, [] { ok = set_smem(fp4_split_kernel<NV, GATED, NT, QX>, C::smem); });
-  if (!ok) return MOE_ERR_CUDA;
+  static ContextCache<bool> cache;
+  bool raised;
+  if (!cache.get(current_context_id, [](bool& v) { return v = set_smem(fp4_split_kernel<NV, GATED, NT, QX>, C::smem); }, raised))
+    return MOE_ERR_CUDA;
   LaunchCfg c(dim3(static_cast<unsigned>(w_tiles * a.t_tiles * a.splits)), kSplitThreads, C::smem, a.splits, true, s);
   if (cudaLaunchKernelEx(&c.cfg, fp4_split_kernel<NV, GATED, NT, QX>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
   note_launch();

@@ -155,6 +155,10 @@ cudaError_t launch_router_backward(const Layout& L, const void* ws, const void* 
                                    const void* w_router, const int32_t* ids, const float* w,
                                    const float* dw, void* dx, float* dw_router, cudaStream_t s);
 
+// Unique id of the calling thread's current CUDA context, never used again for
+// another one; 0 if none is current.
+unsigned long long current_context_id();
+
 // Launch accounting (every kernel launch of the library calls note_launch).
 void note_launch();
 

@@ -339,6 +339,31 @@ cudaError_t launch_build_schedule(const Layout& L, const int32_t* ids, void* ws,
   return launch_build_schedule_with_scratch(L, ids, ws, at<int32_t>(ws, L.warp_counts), s);
 }
 
+// Driver entry points looked up once through the runtime, no libcuda link.
+unsigned long long current_context_id() {
+  typedef CUresult (*GetCurrentFn)(CUcontext*);
+  typedef CUresult (*GetIdFn)(CUcontext, unsigned long long*);
+  static GetCurrentFn get_current = nullptr;
+  static GetIdFn get_id = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess && q == cudaDriverEntryPointSuccess)
+      get_current = reinterpret_cast<GetCurrentFn>(p);
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess && q == cudaDriverEntryPointSuccess)
+      get_id = reinterpret_cast<GetIdFn>(p);
+  });
+  CUcontext ctx = nullptr;
+  unsigned long long id = 0;
+  if (!get_current || !get_id || get_current(&ctx) != CUDA_SUCCESS || ctx == nullptr ||
+      get_id(ctx, &id) != CUDA_SUCCESS)
+    return 0;
+  return id;
+}
+
 }  // namespace moe
 
 // ---------------------------------------------------------------------------
@@ -368,32 +393,6 @@ struct ScratchAddr {
 };
 ScratchAddr g_scratch_addr[kMaxDevices] = {};
 
-// Unique id of the calling thread's current context (driver entry points
-// looked up once through the runtime, no libcuda link); 0 if none is current.
-unsigned long long current_context_id() {
-  typedef CUresult (*GetCurrentFn)(CUcontext*);
-  typedef CUresult (*GetIdFn)(CUcontext, unsigned long long*);
-  static GetCurrentFn get_current = nullptr;
-  static GetIdFn get_id = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess && q == cudaDriverEntryPointSuccess)
-      get_current = reinterpret_cast<GetCurrentFn>(p);
-    if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess && q == cudaDriverEntryPointSuccess)
-      get_id = reinterpret_cast<GetIdFn>(p);
-  });
-  CUcontext ctx = nullptr;
-  unsigned long long id = 0;
-  if (!get_current || !get_id || get_current(&ctx) != CUDA_SUCCESS || ctx == nullptr ||
-      get_id(ctx, &id) != CUDA_SUCCESS)
-    return 0;
-  return id;
-}
-
 // Device address of g_sched_scratch on the current device. In host code the
 // array's name is only a host-side stand-in, so the address is looked up with
 // the device current and cached per device together with the id of the
@@ -405,7 +404,7 @@ cudaError_t scratch_for_current_device(int32_t** out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  const unsigned long long ctx = current_context_id();
+  const unsigned long long ctx = moe::current_context_id();
   std::lock_guard<std::mutex> lock(g_scratch_mu);
   ScratchAddr& c = g_scratch_addr[dev];
   if (ctx == 0 || c.ctx_id != ctx || !c.ptr) {
@@ -413,7 +412,7 @@ cudaError_t scratch_for_current_device(int32_t** out) {
     e = cudaGetSymbolAddress(&p, g_sched_scratch);  // also makes the device's context current
     if (e != cudaSuccess) return e;
     c.ptr = static_cast<int32_t*>(p);
-    c.ctx_id = current_context_id();
+    c.ctx_id = moe::current_context_id();
   }
   *out = c.ptr;
   return cudaSuccess;
