@@ -316,24 +316,30 @@ inline bool tma_map_pitched(CUtensorMap* m, const void* base, int64_t inner, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The status of a runtime call. CUDA keeps an error for whoever asks next, which
+// would be another call's launch check, so it is taken here.
+inline moe_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  (void)cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
 // SMs of the GPU (every GPU of a machine is the same part; asked once).
 inline int device_sms() {
   static const int sms = [] {
     int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    cuda_status(cudaGetDevice(&dev));
+    cuda_status(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
     return n > 0 ? n : 148;
   }();
   return sms;
 }
 
 // Raises a kernel's dynamic shared-memory limit, which holds in the current
-// context only. A refusal is left to the caller, not to the next launch's check.
+// context only.
 template <class K>
 bool set_smem(K kernel, int bytes) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
-  (void)cudaGetLastError();
-  return false;
+  return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) == MOE_OK;
 }
 
 // Microseconds of a split kernel's parts, fitted to a GB300 over 20 to 40 problem
@@ -419,5 +425,13 @@ struct LaunchCfg {
   }
   LaunchCfg(const LaunchCfg&) = delete;
 };
+
+// Launches a kernel and counts it.
+template <class K, class... A>
+moe_status launch_kernel(const LaunchCfg& c, K kernel, const A&... args) {
+  const moe_status st = cuda_status(cudaLaunchKernelEx(&c.cfg, kernel, args...));
+  if (st == MOE_OK) note_launch();
+  return st;
+}
 
 }  // namespace moe

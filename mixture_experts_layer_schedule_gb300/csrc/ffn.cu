@@ -850,10 +850,7 @@ int pair_clusters(int pairs) {
     if (!set_smem(dense_pair_kernel<MODE, KSPLIT>, PCfg<MODE>::smem)) return false;
     for (int p = 1; p <= (KSPLIT ? 4 : 1); ++p) {
       LaunchCfg l(dim3(2 * p), kThreads, PCfg<MODE>::smem, 2 * p, false, nullptr);
-      if (cudaOccupancyMaxActiveClusters(&c.n[p], dense_pair_kernel<MODE, KSPLIT>, &l.cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return false;
-      }
+      if (cuda_status(cudaOccupancyMaxActiveClusters(&c.n[p], dense_pair_kernel<MODE, KSPLIT>, &l.cfg)) != MOE_OK) return false;
     }
     return true;
   }, v);
@@ -866,9 +863,7 @@ moe_status launch_pair_tiles(const DMaps& m, const DArgs& a, cudaStream_t s) {
   const int most = pair_clusters<MODE, false>(1);
   if (most <= 0) return MOE_ERR_CUDA;
   LaunchCfg c(dim3(2 * static_cast<unsigned>(std::min<int64_t>(most, a.tiles))), kThreads, PCfg<MODE>::smem, 2, true, s);
-  if (cudaLaunchKernelEx(&c.cfg, dense_pair_kernel<MODE, false>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
-  note_launch();
-  return MOE_OK;
+  return launch_kernel(c, dense_pair_kernel<MODE, false>, m, a);
 }
 
 // The weight gradients with K split over the pairs of a cluster where that
@@ -887,9 +882,7 @@ moe_status launch_wgrad(const DMaps& m, DArgs a, cudaStream_t s) {
   }
   if (a.splits == 1) return launch_pair_tiles<D_WGRAD>(m, a, s);
   LaunchCfg c(dim3(static_cast<unsigned>(2 * a.splits * a.tiles)), kThreads, PCfg<D_WGRAD>::smem, 2 * a.splits, true, s);
-  if (cudaLaunchKernelEx(&c.cfg, dense_pair_kernel<D_WGRAD, true>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
-  note_launch();
-  return MOE_OK;
+  return launch_kernel(c, dense_pair_kernel<D_WGRAD, true>, m, a);
 }
 
 template <int MODE, int NT>
@@ -899,9 +892,7 @@ moe_status launch_split_nt(const SMaps& m, const DArgs& a, int w_tiles, cudaStre
   if (!cache.get(current_context_id, [](bool& v) { return v = set_smem(dense_split_kernel<MODE, NT>, SplitCfg<NT>::smem); }, raised))
     return MOE_ERR_CUDA;
   LaunchCfg c(dim3(static_cast<unsigned>(w_tiles * a.t_tiles * a.splits)), kSplitThreads, SplitCfg<NT>::smem, a.splits, true, s);
-  if (cudaLaunchKernelEx(&c.cfg, dense_split_kernel<MODE, NT>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
-  note_launch();
-  return MOE_OK;
+  return launch_kernel(c, dense_split_kernel<MODE, NT>, m, a);
 }
 
 template <int MODE>
@@ -1198,19 +1189,15 @@ moe_status ffn_get_device_error(const ffn_problem* p, const void* ws, int32_t* c
   FfnLayout L;
   FFN_TRY(ffn_layout(p, &L));
   if (!al(ws, 256) || !code_out) return MOE_ERR_INVALID_ARG;
-  return cudaMemcpyAsync(code_out, ws, sizeof(int32_t), cudaMemcpyDeviceToHost,
-                         static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  return cuda_status(
+      cudaMemcpyAsync(code_out, ws, sizeof(int32_t), cudaMemcpyDeviceToHost, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status ffn_clear_device_error(const ffn_problem* p, void* ws, void* stream) {
   FfnLayout L;
   FFN_TRY(ffn_layout(p, &L));
   if (!al(ws, 256)) return MOE_ERR_INVALID_ARG;
-  return cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  return cuda_status(cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -221,15 +221,13 @@ moe_status launch_fp4_quantize(const void* src, int32_t elt, int64_t rows, int64
   const dim3 grid(static_cast<unsigned>(std::min(steps, wide)), static_cast<unsigned>(row_groups));
   const NvScale sc = nv_scale(ts);
   const LaunchCfg c(grid, kQThreads, 0, 1, true, st);
-  cudaError_t e = cudaSuccess;
-  auto go = [&](auto kernel) { e = cudaLaunchKernelEx(&c.cfg, kernel, src, ld, rows, cols, kc, sc, q, s); };
+  moe_status status = MOE_OK;
+  auto go = [&](auto kernel) { status = launch_kernel(c, kernel, src, ld, rows, cols, kc, sc, q, s); };
   const bool nv = format == FP4_NV;
   if (elt == MOE_ELT_BF16) nv ? go(fp4_quantize_kernel<MOE_ELT_BF16, true>) : go(fp4_quantize_kernel<MOE_ELT_BF16, false>);
   else if (elt == MOE_ELT_FP16) nv ? go(fp4_quantize_kernel<MOE_ELT_FP16, true>) : go(fp4_quantize_kernel<MOE_ELT_FP16, false>);
   else nv ? go(fp4_quantize_kernel<MOE_ELT_FP32, true>) : go(fp4_quantize_kernel<MOE_ELT_FP32, false>);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  note_launch();
-  return MOE_OK;
+  return status;
 }
 
 }  // namespace moe
@@ -269,17 +267,13 @@ moe_status fp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t format, fl
   const int kc = fp4_quads(format, cols);
   const dim3 grid(static_cast<unsigned>((cols + kQCols - 1) / kQCols), static_cast<unsigned>((rows + 127) / 128 * 4));
   const LaunchCfg c(grid, kQThreads, 0, 1, true, static_cast<cudaStream_t>(stream));
-  cudaError_t e = cudaSuccess;
-  auto go = [&](auto kernel) {
-    e = cudaLaunchKernelEx(&c.cfg, kernel, q, s, rows, cols, kc, tensor_scale, dst, ld);
-  };
+  moe_status status = MOE_OK;
+  auto go = [&](auto kernel) { status = launch_kernel(c, kernel, q, s, rows, cols, kc, tensor_scale, dst, ld); };
   const bool nv = format == FP4_NV;
   if (elt == MOE_ELT_BF16) nv ? go(fp4_dequantize_kernel<MOE_ELT_BF16, true>) : go(fp4_dequantize_kernel<MOE_ELT_BF16, false>);
   else if (elt == MOE_ELT_FP16) nv ? go(fp4_dequantize_kernel<MOE_ELT_FP16, true>) : go(fp4_dequantize_kernel<MOE_ELT_FP16, false>);
   else nv ? go(fp4_dequantize_kernel<MOE_ELT_FP32, true>) : go(fp4_dequantize_kernel<MOE_ELT_FP32, false>);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  note_launch();
-  return MOE_OK;
+  return status;
 }
 
 }  // extern "C"

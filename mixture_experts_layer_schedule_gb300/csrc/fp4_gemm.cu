@@ -740,15 +740,11 @@ moe_status launch_pair(const FMaps& m, const FArgs& a, cudaStream_t s) {
   const bool ok = cache.get(current_context_id, [](int& n) {
     if (!set_smem(fp4_pair_kernel<NV, GATED>, C::smem)) return false;
     LaunchCfg c(dim3(2), C::threads, C::smem, 2, false, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&n, fp4_pair_kernel<NV, GATED>, &c.cfg) == cudaSuccess) return true;
-    (void)cudaGetLastError();
-    return false;
+    return cuda_status(cudaOccupancyMaxActiveClusters(&n, fp4_pair_kernel<NV, GATED>, &c.cfg)) == MOE_OK;
   }, most);
   if (!ok || most <= 0) return MOE_ERR_CUDA;
   LaunchCfg c(dim3(2 * static_cast<unsigned>(std::min<int64_t>(most, a.tiles))), C::threads, C::smem, 2, true, s);
-  if (cudaLaunchKernelEx(&c.cfg, fp4_pair_kernel<NV, GATED>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
-  note_launch();
-  return MOE_OK;
+  return launch_kernel(c, fp4_pair_kernel<NV, GATED>, m, a);
 }
 
 template <bool NV, bool GATED, int NT, bool QX>
@@ -759,9 +755,7 @@ moe_status launch_split_nt(const FMaps& m, FArgs a, int w_tiles, cudaStream_t s)
   if (!cache.get(current_context_id, [](bool& v) { return v = set_smem(fp4_split_kernel<NV, GATED, NT, QX>, C::smem); }, raised))
     return MOE_ERR_CUDA;
   LaunchCfg c(dim3(static_cast<unsigned>(w_tiles * a.t_tiles * a.splits)), kSplitThreads, C::smem, a.splits, true, s);
-  if (cudaLaunchKernelEx(&c.cfg, fp4_split_kernel<NV, GATED, NT, QX>, m, a) != cudaSuccess) return MOE_ERR_CUDA;
-  note_launch();
-  return MOE_OK;
+  return launch_kernel(c, fp4_split_kernel<NV, GATED, NT, QX>, m, a);
 }
 
 inline bool al(const void* p, uintptr_t n) {
@@ -903,10 +897,8 @@ moe_status fp4_get_device_error(const fp4_problem* p, const void* ws, int32_t* c
   const moe_status st = f4_layout(p, &L);
   if (st != MOE_OK) return st;
   if (!al(ws, 256) || !code_out) return MOE_ERR_INVALID_ARG;
-  return cudaMemcpyAsync(code_out, ws, sizeof(int32_t), cudaMemcpyDeviceToHost,
-                         static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  return cuda_status(
+      cudaMemcpyAsync(code_out, ws, sizeof(int32_t), cudaMemcpyDeviceToHost, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status fp4_clear_device_error(const fp4_problem* p, void* ws, void* stream) {
@@ -914,9 +906,7 @@ moe_status fp4_clear_device_error(const fp4_problem* p, void* ws, void* stream) 
   const moe_status st = f4_layout(p, &L);
   if (st != MOE_OK) return st;
   if (!al(ws, 256)) return MOE_ERR_INVALID_ARG;
-  return cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  return cuda_status(cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
