@@ -437,26 +437,42 @@ def ffn_workspace_bytes(p: FFNProblem) -> int:
     return out.value
 
 
-def dense_ptr(name, t, shape, dtype):
-    """Device address of a dense tensor of this shape and type (the front ends'
-    argument check in one pass)."""
+def dense_ptr(name, t, shape, dtype, dev):
+    """Address of a dense tensor of this shape and type on GPU `dev` (the front
+    ends' argument check in one pass; -1: buffers on the host, which the caller refuses)."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of "
                          f"shape {tuple(t.shape)}")
-    if t.is_contiguous() and t.is_cuda:
+    if t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
-    return _ptr(t)  # raises
+    p = _ptr(t)  # raises for a host tensor and for other strides
+    if dev >= 0:
+        raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got one on {t.device}")
+    return p
 
 
-def matrix_ptr(name, t, shape, dtype):
-    """(address, row pitch) of a matrix of this shape and type with dense rows."""
+def matrix_ptr(name, t, shape, dtype, dev):
+    """(address, row pitch) of a matrix of this shape and type with dense rows on GPU `dev`."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of "
                          f"shape {tuple(t.shape)}")
     stride = t.stride()
-    if t.is_cuda and (stride[1] == 1 or shape[1] <= 1):
+    if t.get_device() == dev and (stride[1] == 1 or shape[1] <= 1):
         return t.data_ptr(), (stride[0] if shape[0] > 1 else shape[1])
-    return _mat(t)  # raises
+    p = _mat(t)  # raises for a host tensor and for other strides
+    if dev >= 0:
+        raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got one on {t.device}")
+    return p
+
+
+def stream_on(dev, stream):
+    """Handle of the stream for a call on buffers of GPU `dev`: kernels run on the
+    current device, so it has to be that one."""
+    current = torch._C._cuda_getDevice()
+    if current != dev:
+        raise ValueError(f"the current device is cuda:{current}, the buffers are on cuda:{dev} "
+                         f"(torch.cuda.set_device)")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def ffn_forward(p, x, w_gate, w_up, w_down, g, u, act, y, ws, stream=None):

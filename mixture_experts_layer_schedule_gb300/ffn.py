@@ -59,7 +59,7 @@ class GatedFFN:
         dev = torch.device(device)
         self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)  # clears the error word
         self.y = torch.empty((N, H), dtype=dtype, device=dev)
-        self._cuda = self.y.is_cuda
+        self._dev = self.y.get_device()  # -1 on the host
         self.g = self.u = self.a = self.grads = None
         if training:
             self.g, self.u, self.a = (torch.empty((N, I), dtype=dtype, device=dev) for _ in range(3))
@@ -69,16 +69,17 @@ class GatedFFN:
                                   dw_down=torch.empty((H, I), dtype=grad_dtype, device=dev))
 
     def _weights(self, wg, wu, wd):
-        if not self._cuda:  # kernels would fault on host addresses
+        if self._dev < 0:  # kernels would fault on host addresses
             raise ValueError("expected a GatedFFN on a CUDA device")
-        return (dense_ptr("wg", wg, self._w_in, self.dtype), dense_ptr("wu", wu, self._w_in, self.dtype),
-                dense_ptr("wd", wd, self._w_out, self.dtype))
+        return (dense_ptr("wg", wg, self._w_in, self.dtype, self._dev),
+                dense_ptr("wu", wu, self._w_in, self.dtype, self._dev),
+                dense_ptr("wd", wd, self._w_out, self.dtype, self._dev))
 
     def _forward(self, x, wg, wu, wd, saved, stream):
-        xp, ldx = matrix_ptr("x", x, self._tokens, self.dtype)
+        xp, ldx = matrix_ptr("x", x, self._tokens, self.dtype, self._dev)
         y = self.y
         _lib._call("ffn_forward", self._p, xp, ldx, *self._weights(wg, wu, wd), *saved, y.data_ptr(),
-                   self.H, self.ws.data_ptr(), _lib._stream(stream))
+                   self.H, self.ws.data_ptr(), _lib.stream_on(self._dev, stream))
         return y
 
     def forward(self, x, wg, wu, wd, stream=None):
@@ -99,13 +100,14 @@ class GatedFFN:
         d = self.grads
         if d is None:
             raise ValueError("backward() needs training=True")
-        xp, ldx = matrix_ptr("x", x, self._tokens, self.dtype)
-        dyp, lddy = matrix_ptr("dy", dy, self._tokens, self.dtype)
+        xp, ldx = matrix_ptr("x", x, self._tokens, self.dtype, self._dev)
+        dyp, lddy = matrix_ptr("dy", dy, self._tokens, self.dtype, self._dev)
         g, u, a = (self.g, self.u, self.a) if saved is None else saved
-        _lib._call("ffn_backward", self._p, xp, ldx, dense_ptr("g", g, self._inner, self.dtype),
-                   dense_ptr("u", u, self._inner, self.dtype), dense_ptr("a", a, self._inner, self.dtype),
+        inner, dtype, dev = self._inner, self.dtype, self._dev
+        _lib._call("ffn_backward", self._p, xp, ldx, dense_ptr("g", g, inner, dtype, dev),
+                   dense_ptr("u", u, inner, dtype, dev), dense_ptr("a", a, inner, dtype, dev),
                    *self._weights(wg, wu, wd), dyp, lddy, d.dx.data_ptr(), self.H, d.dw_gate.data_ptr(),
-                   d.dw_up.data_ptr(), d.dw_down.data_ptr(), self.ws.data_ptr(), _lib._stream(stream))
+                   d.dw_up.data_ptr(), d.dw_down.data_ptr(), self.ws.data_ptr(), _lib.stream_on(self._dev, stream))
         return d
 
     def device_error(self, stream=None) -> int:

@@ -45,7 +45,7 @@ class FP4Tensor:
         self.operand = _lib.FP4Operand(self._q.data_ptr(), self._s.data_ptr(), 1.0)
         self.scale = scale
         self._shape, self._operand = (self.rows, self.cols), ctypes.byref(self.operand)
-        self._cuda = self._q.is_cuda
+        self._dev = self._q.get_device()  # -1 on the host
 
     @property
     def scale(self) -> float:
@@ -99,16 +99,16 @@ class FP4Tensor:
 
     def on_device(self):
         """Raises unless the buffers are on the GPU (kernels would fault on host addresses)."""
-        if not self._cuda:
+        if self._dev < 0:
             raise ValueError("expected an FP4Tensor on a CUDA device")
 
     def quantize(self, src, stream=None) -> "FP4Tensor":
         """Codes and scales of src (bf16, fp16 or fp32; rows may be strided)."""
         elt = _elt(src)
-        sp, ld = matrix_ptr("src", src, self._shape, src.dtype)
+        sp, ld = matrix_ptr("src", src, self._shape, src.dtype, self._dev)
         self.on_device()
         _lib._call("fp4_quantize", sp, elt, self.rows, self.cols, ld, self.format, self.scale,
-                   self.operand.q, self.operand.s, _lib._stream(stream))
+                   self.operand.q, self.operand.s, _lib.stream_on(self._dev, stream))
         return self
 
     def dequantize(self, out=None, dtype=torch.bfloat16, stream=None):
@@ -118,10 +118,10 @@ class FP4Tensor:
             with _lib.stream_scope(stream):
                 out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.q.device)
         elt = _elt(out)
-        op, ld = matrix_ptr("out", out, self._shape, out.dtype)
+        op, ld = matrix_ptr("out", out, self._shape, out.dtype, self._dev)
         self.on_device()
         _lib._call("fp4_dequantize", self.operand.q, self.operand.s, self.format, self.scale, self.rows,
-                   self.cols, op, elt, ld, _lib._stream(stream))
+                   self.cols, op, elt, ld, _lib.stream_on(self._dev, stream))
         return out
 
 
@@ -144,30 +144,32 @@ class FP4Linear:
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self.ws[:256].zero_()  # clears the device error word
         self.y = torch.empty((self.M, self.N), dtype=dtype, device=dev)
-        self._cuda = self.y.is_cuda
+        self._dev = self.y.get_device()  # -1 on the host
 
     def _weight(self, w):
-        if not self._cuda:
+        if self._dev < 0:
             raise ValueError("expected an FP4Linear on a CUDA device")
         if w._shape != self._w_shape or w.format != self.format:
             raise ValueError(f"weights [{w.rows}, {w.cols}] of format {w.format}: expected "
                              f"[{self.N}, {self.K}] of format {self.format}")
-        w.on_device()
+        if w._dev != self._dev:
+            w.on_device()
+            raise ValueError(f"weights on cuda:{w._dev}: expected them on cuda:{self._dev}")
         return w._operand
 
     def forward(self, x, w: FP4Tensor, stream=None):
         """x w^T."""
-        xp, ldx = matrix_ptr("x", x, self._x_shape, self.dtype)
+        xp, ldx = matrix_ptr("x", x, self._x_shape, self.dtype, self._dev)
         _lib._call("fp4_linear", self._p, xp, ldx, self.x_scale, self._weight(w), self.y.data_ptr(),
-                   self.N, self.ws.data_ptr(), _lib._stream(stream))
+                   self.N, self.ws.data_ptr(), _lib.stream_on(self._dev, stream))
         return self.y
 
     def forward_gated(self, x, w_gate: FP4Tensor, w_up: FP4Tensor, stream=None):
         """h(x w_gate^T) * (x w_up^T), h the activation."""
-        xp, ldx = matrix_ptr("x", x, self._x_shape, self.dtype)
+        xp, ldx = matrix_ptr("x", x, self._x_shape, self.dtype, self._dev)
         _lib._call("fp4_gated_linear", self._p, xp, ldx, self.x_scale, self._weight(w_gate),
                    self._weight(w_up), self.y.data_ptr(), self.N, self.ws.data_ptr(),
-                   _lib._stream(stream))
+                   _lib.stream_on(self._dev, stream))
         return self.y
 
     def device_error(self, stream=None) -> int:
