@@ -475,23 +475,6 @@ def stream_on(dev, stream):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def ffn_forward(p, x, w_gate, w_up, w_down, g, u, act, y, ws, stream=None):
-    xp, ldx = _mat(x)
-    yp, ldy = _mat(y)
-    _call("ffn_forward", ctypes.byref(p), xp, ldx, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(g),
-          _ptr(u), _ptr(act), yp, ldy, _ptr(ws), _stream(stream))
-
-
-def ffn_backward(p, x, g, u, act, w_gate, w_up, w_down, dy, dx, dw_gate, dw_up, dw_down, ws,
-                 stream=None):
-    xp, ldx = _mat(x)
-    dyp, lddy = _mat(dy)
-    dxp, lddx = _mat(dx)
-    _call("ffn_backward", ctypes.byref(p), xp, ldx, _ptr(g), _ptr(u), _ptr(act), _ptr(w_gate),
-          _ptr(w_up), _ptr(w_down), dyp, lddy, dxp, lddx, _ptr(dw_gate), _ptr(dw_up),
-          _ptr(dw_down), _ptr(ws), _stream(stream))
-
-
 def ffn_get_device_error(p, ws, stream=None) -> int:
     """Reads the device error word of an ffn workspace (synchronises the stream)."""
     return _read_error("ffn_get_device_error", p, ws, stream)
@@ -505,46 +488,16 @@ def fp4_problem(M, N, K, format=FP4_NV, elt=MOE_ELT_BF16, act=FFN_SILU, kernel=0
     return FP4Problem(int(M), int(N), int(K), int(format), int(elt), int(act), int(kernel))
 
 
-def fp4_operand(q, s, scale=1.0) -> FP4Operand:
-    return FP4Operand(_ptr(q), _ptr(s), float(scale))
-
-
 def fp4_scale_bytes(format, rows, cols) -> int:
     out = c_sz(0)
     _call("fp4_scale_bytes", int(format), int(rows), int(cols), ctypes.byref(out))
     return out.value
 
 
-def fp4_quantize(src, elt, rows, cols, format, tensor_scale, q, s, stream=None):
-    sp, ld = _mat(src)
-    _call("fp4_quantize", sp, int(elt), int(rows), int(cols), ld, int(format), float(tensor_scale),
-          _ptr(q), _ptr(s), _stream(stream))
-
-
-def fp4_dequantize(q, s, format, tensor_scale, rows, cols, dst, elt, stream=None):
-    dp, ld = _mat(dst)
-    _call("fp4_dequantize", _ptr(q), _ptr(s), int(format), float(tensor_scale), int(rows),
-          int(cols), dp, int(elt), ld, _stream(stream))
-
-
 def fp4_workspace_bytes(p: FP4Problem) -> int:
     out = c_sz(0)
     _call("fp4_workspace_bytes", ctypes.byref(p), ctypes.byref(out))
     return out.value
-
-
-def fp4_linear(p, x, x_scale, w: FP4Operand, y, ws, stream=None):
-    xp, ldx = _mat(x)
-    yp, ldy = _mat(y)
-    _call("fp4_linear", ctypes.byref(p), xp, ldx, float(x_scale), ctypes.byref(w), yp, ldy, _ptr(ws),
-          _stream(stream))
-
-
-def fp4_gated_linear(p, x, x_scale, w_gate: FP4Operand, w_up: FP4Operand, y, ws, stream=None):
-    xp, ldx = _mat(x)
-    yp, ldy = _mat(y)
-    _call("fp4_gated_linear", ctypes.byref(p), xp, ldx, float(x_scale), ctypes.byref(w_gate),
-          ctypes.byref(w_up), yp, ldy, _ptr(ws), _stream(stream))
 
 
 def fp4_get_device_error(p, ws, stream=None) -> int:
