@@ -324,6 +324,10 @@ inline moe_status cuda_status(cudaError_t e) {
   return MOE_ERR_CUDA;
 }
 
+inline bool aligned(const void* p, uintptr_t n) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
 // SMs of the GPU (every GPU of a machine is the same part; asked once).
 inline int device_sms() {
   static const int sms = [] {

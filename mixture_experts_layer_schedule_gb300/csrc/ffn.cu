@@ -951,11 +951,8 @@ moe_status ffn_layout(const ffn_problem* p, FfnLayout* L) {
   return MOE_OK;
 }
 
-inline bool al(const void* p, uintptr_t a) {
-  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
 // A pitched 16-bit matrix of `cols` columns (16-byte rows).
-inline bool mat(const void* p, int64_t ld, int64_t cols) { return al(p, 16) && ld >= cols && ld % 8 == 0; }
+inline bool mat(const void* p, int64_t ld, int64_t cols) { return aligned(p, 16) && ld >= cols && ld % 8 == 0; }
 
 // The split kernel's launch for a product over nkb k-blocks with w_tiles weight
 // tiles, and whether it serves the product against `pair_tiles` 256 x 256 tiles
@@ -1153,10 +1150,11 @@ moe_status ffn_forward(const ffn_problem* p, const void* x, int64_t ldx, const v
                        int64_t ldy, void* ws, void* stream) {
   FfnLayout L;
   FFN_TRY(ffn_layout(p, &L));
-  if (!al(ws, 256) || !al(w_gate, 16) || !al(w_up, 16) || !al(w_down, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(ws, 256) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(w_down, 16)) return MOE_ERR_INVALID_ARG;
   if ((g == nullptr) != (u == nullptr) || (g && !act)) return MOE_ERR_INVALID_ARG;
   if (L.N == 0) return MOE_OK;
-  if (!mat(x, ldx, L.H) || !mat(y, ldy, L.H) || (g && (!al(g, 16) || !al(u, 16))) || (act && !al(act, 16)))
+  if (!mat(x, ldx, L.H) || !mat(y, ldy, L.H) || (g && (!aligned(g, 16) || !aligned(u, 16))) ||
+      (act && !aligned(act, 16)))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* a = act ? act : at<char>(ws, L.dg);
@@ -1170,11 +1168,11 @@ moe_status ffn_backward(const ffn_problem* p, const void* x, int64_t ldx, const 
                         void* dw_up, void* dw_down, void* ws, void* stream) {
   FfnLayout L;
   FFN_TRY(ffn_layout(p, &L));
-  if (!al(ws, 256) || !al(w_gate, 16) || !al(w_up, 16) || !al(w_down, 16) || !al(dw_gate, 16) ||
-      !al(dw_up, 16) || !al(dw_down, 16))
+  if (!aligned(ws, 256) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(w_down, 16) || !aligned(dw_gate, 16) ||
+      !aligned(dw_up, 16) || !aligned(dw_down, 16))
     return MOE_ERR_INVALID_ARG;
-  if (L.N > 0 && (!mat(x, ldx, L.H) || !mat(dy, lddy, L.H) || !mat(dx, lddx, L.H) || !al(g, 16) ||
-                  !al(u, 16) || !al(act, 16)))
+  if (L.N > 0 && (!mat(x, ldx, L.H) || !mat(dy, lddy, L.H) || !mat(dx, lddx, L.H) || !aligned(g, 16) ||
+                  !aligned(u, 16) || !aligned(act, 16)))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void *dg = at<char>(ws, L.dg), *du = at<char>(ws, L.du);
@@ -1188,7 +1186,7 @@ moe_status ffn_backward(const ffn_problem* p, const void* x, int64_t ldx, const 
 moe_status ffn_get_device_error(const ffn_problem* p, const void* ws, int32_t* code_out, void* stream) {
   FfnLayout L;
   FFN_TRY(ffn_layout(p, &L));
-  if (!al(ws, 256) || !code_out) return MOE_ERR_INVALID_ARG;
+  if (!aligned(ws, 256) || !code_out) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       cudaMemcpyAsync(code_out, ws, sizeof(int32_t), cudaMemcpyDeviceToHost, static_cast<cudaStream_t>(stream)));
 }
@@ -1196,7 +1194,7 @@ moe_status ffn_get_device_error(const ffn_problem* p, const void* ws, int32_t* c
 moe_status ffn_clear_device_error(const ffn_problem* p, void* ws, void* stream) {
   FfnLayout L;
   FFN_TRY(ffn_layout(p, &L));
-  if (!al(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   return cuda_status(cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
 }
 

@@ -184,11 +184,9 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t
   }
 }
 
-inline bool al16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // Row pitch and alignment of a matrix of `elt` values: 16-byte rows.
 bool matrix_ok(const void* p, int64_t ld, int64_t cols, int32_t elt) {
-  return al16(p) && ld >= cols && ld % (elt == MOE_ELT_FP32 ? 4 : 8) == 0;
+  return aligned(p, 16) && ld >= cols && ld % (elt == MOE_ELT_FP32 ? 4 : 8) == 0;
 }
 
 }  // namespace
@@ -251,7 +249,7 @@ moe_status fp4_quantize(const void* src, int32_t elt, int64_t rows, int64_t cols
   if (elt < MOE_ELT_BF16 || elt > MOE_ELT_FP32) return MOE_ERR_UNSUPPORTED;
   if (!fp4_scale_ok(format, tensor_scale)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!matrix_ok(src, ld, cols, elt) || !al16(q) || !al16(s)) return MOE_ERR_INVALID_ARG;
+  if (!matrix_ok(src, ld, cols, elt) || !aligned(q, 16) || !aligned(s, 16)) return MOE_ERR_INVALID_ARG;
   return launch_fp4_quantize(src, elt, rows, cols, ld, format, tensor_scale, q, s,
                              static_cast<cudaStream_t>(stream));
 }
@@ -263,7 +261,7 @@ moe_status fp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t format, fl
   if (elt < MOE_ELT_BF16 || elt > MOE_ELT_FP32) return MOE_ERR_UNSUPPORTED;
   if (!fp4_scale_ok(format, tensor_scale)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!matrix_ok(dst, ld, cols, elt) || !al16(q) || !al16(s)) return MOE_ERR_INVALID_ARG;
+  if (!matrix_ok(dst, ld, cols, elt) || !aligned(q, 16) || !aligned(s, 16)) return MOE_ERR_INVALID_ARG;
   const int kc = fp4_quads(format, cols);
   const dim3 grid(static_cast<unsigned>((cols + kQCols - 1) / kQCols), static_cast<unsigned>((rows + 127) / 128 * 4));
   const LaunchCfg c(grid, kQThreads, 0, 1, true, static_cast<cudaStream_t>(stream));

@@ -758,10 +758,6 @@ moe_status launch_split_nt(const FMaps& m, FArgs a, int w_tiles, cudaStream_t s)
   return launch_kernel(c, fp4_split_kernel<NV, GATED, NT, QX>, m, a);
 }
 
-inline bool al(const void* p, uintptr_t n) {
-  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
-}
-
 struct F4Layout {
   size_t q, s, bytes;
 };
@@ -782,7 +778,7 @@ moe_status f4_layout(const fp4_problem* p, F4Layout* L) {
 }
 
 bool operand_ok(const fp4_operand* w, int32_t format) {
-  return w && al(w->q, 16) && al(w->s, 16) && fp4_scale_ok(format, w->scale);
+  return w && aligned(w->q, 16) && aligned(w->s, 16) && fp4_scale_ok(format, w->scale);
 }
 
 template <bool NV, bool GATED>
@@ -851,11 +847,11 @@ moe_status checked(const fp4_problem* p, const void* x, int64_t ldx, float x_sca
   F4Layout L;
   const moe_status st = f4_layout(p, &L);
   if (st != MOE_OK) return st;
-  if (!al(ws, 256) || !operand_ok(w0, p->format) || (gated && !operand_ok(w1, p->format)) ||
+  if (!aligned(ws, 256) || !operand_ok(w0, p->format) || (gated && !operand_ok(w1, p->format)) ||
       !fp4_scale_ok(p->format, x_scale))
     return MOE_ERR_INVALID_ARG;
   if (p->M == 0) return MOE_OK;
-  if (!al(x, 16) || ldx < p->K || ldx % 8 != 0 || !al(y, 16) || ldy < p->N || ldy % 8 != 0)
+  if (!aligned(x, 16) || ldx < p->K || ldx % 8 != 0 || !aligned(y, 16) || ldy < p->N || ldy % 8 != 0)
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p->format == FP4_NV)
@@ -896,7 +892,7 @@ moe_status fp4_get_device_error(const fp4_problem* p, const void* ws, int32_t* c
   F4Layout L;
   const moe_status st = f4_layout(p, &L);
   if (st != MOE_OK) return st;
-  if (!al(ws, 256) || !code_out) return MOE_ERR_INVALID_ARG;
+  if (!aligned(ws, 256) || !code_out) return MOE_ERR_INVALID_ARG;
   return cuda_status(
       cudaMemcpyAsync(code_out, ws, sizeof(int32_t), cudaMemcpyDeviceToHost, static_cast<cudaStream_t>(stream)));
 }
@@ -905,7 +901,7 @@ moe_status fp4_clear_device_error(const fp4_problem* p, void* ws, void* stream) 
   F4Layout L;
   const moe_status st = f4_layout(p, &L);
   if (st != MOE_OK) return st;
-  if (!al(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   return cuda_status(cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
 }
 
