@@ -453,7 +453,8 @@ moe_status mxfp8_qdq(const void* src_bf16, void* dst_bf16, int64_t rows, int64_t
  * (w_gate, w_up [I][H], w_down [H][I]). Activations, weights and outputs are
  * bf16 or fp16, sums are fp32. x, y, dy, dx are row-major with a row pitch of
  * ld* elements (a multiple of 8, at least H); G, U, A and the weights are dense.
- * Every matrix 16-byte aligned, none overlapping an output. ws: 256-byte
+ * Every matrix 16-byte aligned, none overlapping an output, except that y may
+ * overlap x and dx may overlap x or dy. ws: 256-byte
  * aligned, ffn_workspace_bytes bytes, its first int32 the device error word
  * (zero it once); calls that share a workspace must not overlap on the GPU. */
 typedef enum { MOE_ELT_BF16 = 0, MOE_ELT_FP16 = 1, MOE_ELT_FP32 = 2 } moe_elt;

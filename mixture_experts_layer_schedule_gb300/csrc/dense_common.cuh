@@ -328,6 +328,13 @@ inline bool aligned(const void* p, uintptr_t n) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+// Whether two pitched 16-bit matrices [rows][cols] share an address range.
+inline bool overlap(const void* a, int64_t lda, int64_t cols_a, const void* b, int64_t ldb, int64_t cols_b,
+                    int64_t rows) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + 2 * ((rows - 1) * ldb + cols_b) && b0 < a0 + 2 * ((rows - 1) * lda + cols_a);
+}
+
 // SMs of the GPU (every GPU of a machine is the same part; asked once).
 inline int device_sms() {
   static const int sms = [] {

@@ -1176,11 +1176,16 @@ moe_status ffn_backward(const ffn_problem* p, const void* x, int64_t ldx, const 
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void *dg = at<char>(ws, L.dg), *du = at<char>(ws, L.du);
-  if (L.N > 0) {
-    FFN_TRY(run_dact(p, dy, lddy, w_down, g, u, dg, du, ws, s));
-    FFN_TRY(run_dx(p, dg, du, w_gate, w_up, dx, lddx, ws, s));
-  }
-  return run_wgrad(p, x, ldx, act, dy, lddy, dg, du, dw_gate, dw_up, dw_down, ws, s);
+  auto wgrad = [&] { return run_wgrad(p, x, ldx, act, dy, lddy, dg, du, dw_gate, dw_up, dw_down, ws, s); };
+  if (L.N == 0) return wgrad();
+  FFN_TRY(run_dact(p, dy, lddy, w_down, g, u, dg, du, ws, s));
+  // dX and the weight gradients need dG and dU and not each other. The latter read
+  // x and dy: before dX where it is written over one of them (one object whose dx
+  // is handed on as the next layer's dy).
+  const bool late = overlap(dx, lddx, L.H, dy, lddy, L.H, L.N) || overlap(dx, lddx, L.H, x, ldx, L.H, L.N);
+  if (late) FFN_TRY(wgrad());
+  FFN_TRY(run_dx(p, dg, du, w_gate, w_up, dx, lddx, ws, s));
+  return late ? MOE_OK : wgrad();
 }
 
 moe_status ffn_get_device_error(const ffn_problem* p, const void* ws, int32_t* code_out, void* stream) {
