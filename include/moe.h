@@ -528,9 +528,9 @@ moe_status fp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t format, fl
  * with tensor scale x_scale; weights [N, K] come from fp4_quantize.
  *   fp4_linear        y = dq(q(X)) dq(W)^T
  *   fp4_gated_linear  y = h(dq(q(X)) dq(Wg)^T) * (dq(q(X)) dq(Wu)^T)
- * M >= 0; K a multiple of 32, N of 8; act, kernel as in ffn_problem. ws:
- * fp4_workspace_bytes bytes, rules as for an ffn workspace. A non-finite X
- * value makes its row's outputs NaN. */
+ * M >= 0; K a multiple of 32, N of 8; act, kernel as in ffn_problem; y may
+ * overlap x. ws: fp4_workspace_bytes bytes, rules as for an ffn workspace. A
+ * non-finite X value makes its row's outputs NaN. */
 typedef struct {
   int64_t M;
   int32_t N, K;

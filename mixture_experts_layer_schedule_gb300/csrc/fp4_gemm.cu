@@ -809,7 +809,8 @@ moe_status product(const fp4_problem* p, const F4Layout& L, const void* x, int64
   cost.quantise = 0.0;
   SplitPlan big = plan_split(p->M, w_tiles, a.nkb, cost, 64, 128, 64);
   big.us += GATED ? 1.9 : 1.0;
-  if (big.us < sp.us) sp = big;
+  // A product that quantises X itself reads it while other CTAs already store Y.
+  if (big.us < sp.us || overlap(x, ldx, p->K, y, ldy, p->N, p->M)) sp = big;
   const bool split = p->kernel ? p->kernel == 2 : sp.us <= pair_time(a.tiles, a.nkb, GATED ? 5.2 : 3.6, GATED ? 1.5 : 2.6);
   const int64_t t_tiles = (p->M + sp.nt - 1) / sp.nt;
   if (split && t_tiles * w_tiles * 8 > INT32_MAX) return MOE_ERR_UNSUPPORTED;  // grid x

@@ -1,16 +1,47 @@
 """Calls whose operand is the object's own result, which the call writes: they come up
 when one object serves several layers and the result of one call is handed to the
-next. The results are those of calls with a copy."""
+next. The results are those of calls with a copy, up to the order of fp32 sums where
+another kernel is chosen (the bounds of test_gpu_fp4.py)."""
 import pytest
 import torch
 
-from mixture_experts_layer_schedule_gb300 import GatedFFN
+from mixture_experts_layer_schedule_gb300 import FP4Linear, GatedFFN
 
+import test_gpu_fp4 as fp4
 from gpu_helpers import dev
+from test_gpu_ffn import E32, act64, rounding
 
 pytestmark = pytest.mark.gpu
 
 BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M", [1, 5, 32, 77, 700])
+def test_4_bit_products_of_their_own_result(M, fmt):
+    """Wide enough that many CTAs read x while others are through."""
+    K = N = 4096
+    x, xq, (w0, w1), (d0, d1) = fp4.operands(M, N, K, fmt, BF, M, 2)
+    lin = FP4Linear(M, N, K, format=fmt)
+    g, eg = xq @ d0.t(), E32 * (xq.abs() @ d0.abs().t())
+    u, eu = xq @ d1.t(), E32 * (xq.abs() @ d1.abs().t())
+    h, _ = act64(g, "silu")
+    for _ in range(5):
+        lin.y.copy_(x)
+        fp4.check(lin.forward(lin.y, w0), g, rounding(g, BF) + eg)
+        lin.y.copy_(x)
+        fp4.check(lin.forward_gated(lin.y, w0, w1), h * u,
+                  rounding(h * u, BF) + 1.2 * (u.abs() * eg + h.abs() * eu) + E32 * (h * u).abs())
+    assert lin.device_error() == 0
+
+
+def test_4_bit_product_of_a_part_of_its_result():
+    M, N, K = 3, 512, 256
+    x, xq, (w,), (d,) = fp4.operands(M, N, K, "nvfp4", BF, 2, 1)
+    lin = FP4Linear(M, N, K)
+    lin.y[:, K:].copy_(x)
+    y = lin.forward(lin.y[:, K:], w)
+    fp4.check(y, xq @ d.t(), rounding(xq @ d.t(), BF) + E32 * (xq.abs() @ d.abs().t()))
 
 
 @pytest.mark.parametrize("kernel", [1, 2])
