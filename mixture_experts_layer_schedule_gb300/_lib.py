@@ -426,8 +426,16 @@ def mxfp8_qdq(src, dst, rows, cols, axis, stream=None):
     _call("mxfp8_qdq", _ptr(src), _ptr(dst), int(rows), int(cols), int(axis), _stream(stream))
 
 
+def _int32(name, value) -> int:
+    """A size that the ABI holds in 32 bits: ctypes would drop the bits above them."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} = {value}: outside 32 bits")
+    return value
+
+
 def ffn_problem(N, H, I, elt=MOE_ELT_BF16, act=FFN_SILU, grad_elt=None, kernel=0) -> FFNProblem:
-    return FFNProblem(int(N), int(H), int(I), int(elt), int(act),
+    return FFNProblem(int(N), _int32("H", H), _int32("I", I), int(elt), int(act),
                       int(elt if grad_elt is None else grad_elt), int(kernel))
 
 
@@ -485,7 +493,7 @@ def ffn_clear_device_error(p, ws, stream=None):
 
 
 def fp4_problem(M, N, K, format=FP4_NV, elt=MOE_ELT_BF16, act=FFN_SILU, kernel=0) -> FP4Problem:
-    return FP4Problem(int(M), int(N), int(K), int(format), int(elt), int(act), int(kernel))
+    return FP4Problem(int(M), _int32("N", N), _int32("K", K), int(format), int(elt), int(act), int(kernel))
 
 
 def fp4_scale_bytes(format, rows, cols) -> int:
