@@ -449,9 +449,12 @@ moe_status mxfp8_qdq(const void* src_bf16, void* dst_bf16, int64_t rows, int64_t
  * beside the routed ones, or a dense layer); no routing, no schedule. With
  * h = silu or gelu (tanh form):
  *   G = X Wg^T, U = X Wu^T, A = h(G) * U, Y = A Wd^T.
- * Any N >= 0; H and I multiples of 8; weights as in moe_weights with E = 1
+ * Any N from 0 to 2^31 - 512; H and I multiples of 8, at most 2^24; weights as
+ * in moe_weights with E = 1
  * (w_gate, w_up [I][H], w_down [H][I]). Activations, weights and outputs are
- * bf16 or fp16, sums are fp32. x, y, dy, dx are row-major with a row pitch of
+ * bf16 or fp16, sums are fp32. G, U, A, dG and dU pass through that type: in fp16
+ * an inner value above 65504 becomes an infinity, also where A is not stored.
+ * x, y, dy, dx are row-major with a row pitch of
  * ld* elements (a multiple of 8, at least H); G, U, A and the weights are dense.
  * Every matrix 16-byte aligned, none overlapping an output, except that y may
  * overlap x and dx may overlap x or dy. ws: 256-byte
@@ -504,7 +507,8 @@ moe_status ffn_clear_device_error(const ffn_problem* p, void* ws, void* stream);
  * code = v / step rounded to nearest even, saturating at 6; a zero step gives
  * zeros. A block with an infinity or a NaN gets the NaN scale (0xFF / 0x7F):
  * it reads back, and multiplies, as NaN. tensor_scale: 2^-60 to 2^60 (FP4_MX: 1).
- * Matrices are [rows, cols] with cols a multiple of 32, any rows >= 0.
+ * Matrices are [rows, cols], cols a multiple of 32 (at most 2^24), rows from 0
+ * to 2097024 (16383 * 128).
  * q [rows][cols / 2]: two codes to a byte, the even column in the low nibble.
  * s: scales in 512-byte chunks of 128 rows x 4 scales, chunk (row block rb,
  * quad kc) at (rb * KC + kc) * 512, KC = ceil(cols / 64) (FP4_NV) or
@@ -528,8 +532,8 @@ moe_status fp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t format, fl
  * with tensor scale x_scale; weights [N, K] come from fp4_quantize.
  *   fp4_linear        y = dq(q(X)) dq(W)^T
  *   fp4_gated_linear  y = h(dq(q(X)) dq(Wg)^T) * (dq(q(X)) dq(Wu)^T)
- * M >= 0; K a multiple of 32, N of 8; act, kernel as in ffn_problem; y may
- * overlap x. ws: fp4_workspace_bytes bytes, rules as for an ffn workspace. A
+ * M rows and K columns as above, N a multiple of 8; act, kernel as in
+ * ffn_problem; y may overlap x. ws: fp4_workspace_bytes bytes, rules as for an ffn workspace. A
  * non-finite X value makes its row's outputs NaN. */
 typedef struct {
   int64_t M;

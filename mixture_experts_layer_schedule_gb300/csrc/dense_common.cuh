@@ -68,8 +68,11 @@ __device__ __forceinline__ int warp_index() { return __shfl_sync(~0u, static_cas
 // The barrier before a cluster's CTAs leave: they wait for each other, but pass
 // no data, so this thread's stores to global memory need not have arrived (a
 // releasing arrive waits for them, most of a microsecond at the end of every
-// launch). What must be over, it is: values read from other CTAs have gone into
-// stores issued before.
+// launch). Reads of another CTA's partial sums are over when a thread arrives, by
+// data dependence and not by the memory model: every value read goes into the
+// operand of a store that the thread issues before the arrive (the asm's memory
+// clobber keeps that order), and a store cannot issue before its operand is there.
+// Code that reads another CTA's memory for anything else needs the releasing form.
 __device__ __forceinline__ void cluster_leave() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -353,10 +356,13 @@ bool set_smem(K kernel, int bytes) {
   return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) == MOE_OK;
 }
 
-// Microseconds of a split kernel's parts, fitted to a GB300 over 20 to 40 problem
-// sizes (1 to 4096 tokens) with every tile size and cluster size (about 300 to 900
-// launches for each kind of product, 10 to 14% rms; the shapes chosen by it are 1
-// to 3% slower than the best ones of each problem). KB: a stage's kilobytes.
+// Microseconds of a split kernel's parts, fitted to a GB300 over 20 to 24 problem
+// sizes (1 to 4096 tokens) with every tile size and cluster size: about 170 to 380
+// launches for each kind of product, and 130 with weights from HBM for the dense
+// ones. The model is off by 10 to 15% rms. Of the launch shapes of a problem, the
+// one that it picks is 2 to 4% slower than the best on average, 15% at worst for the
+// dense products (400 tokens, 4096 x 512) and 22% for the 4-bit ones (512 tokens, 1536
+// wide, K = 4096). KB: a stage's kilobytes.
 struct SplitCost {
   double w_kb;               // KB of weights and scales per k-block
   double alone;              // per k-block, one CTA on an SM (or 0.0083 per KB: 120 GB/s into it)

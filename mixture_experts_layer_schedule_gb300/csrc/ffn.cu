@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   // Both CTAs are through: the even CTA's MMAs into this CTA's tensor memory have
-  // retired, and nothing signals or reads a CTA that may leave.
+  // retired, and nothing signals a CTA that may leave, or (KSPLIT) reads its partial
+  // sums: see cluster_leave.
   cluster_leave();
   if (warp == 1) {
     tc_fence_after();
@@ -829,7 +830,9 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   if (splits > 1) {
     __syncwarp();
-    cluster_leave();  // no CTA leaves while its partial sums may still be read
+    // No CTA leaves while its partial sums may still be read. The barrier is
+    // relaxed; see cluster_leave for why that is enough here.
+    cluster_leave();
   }
 }
 

@@ -28,9 +28,11 @@
 //    epilogue warps in the linear kernel (63.6 us), output by plain stores
 //    (59.8 us).
 //  * fp4_split_kernel: weight rows on M, 16 to 128 tokens on N, K split over
-//    the CTAs of a cluster (see dense_split_kernel in ffn.cu). Up to 32 tokens
-//    it quantises X itself; above, its weight tiles and scales are fetched while
-//    the quantiser of X still runs. Bound by the latency of one launch: one token
+//    the CTAs of a cluster (see dense_split_kernel in ffn.cu). Tiles of up to 32
+//    tokens quantise X themselves; for tiles of 64 or 128 a quantiser runs first, and
+//    the weight tiles and scales are fetched while it does. The plan takes the former
+//    for few tokens (up to 32 at 4096 x 1536, up to 10 at 4096 x 7168) and for more
+//    where the weights are small. Bound by the latency of one launch: one token
 //    through 4096 x 1536 (3.5 MB) in 3.2 us, gated 1536, K = 4096 (7.1 MB) in
 //    4.1 us; 64 tokens through 7168 x 2048 in 6 us.
 #include <algorithm>
@@ -725,7 +727,9 @@ __global__ void __launch_bounds__(kSplitThreads) fp4_split_kernel(const __grid_c
   }
   if (splits > 1) {
     __syncwarp();
-    cluster_leave();  // no CTA leaves while its partial sums may still be read
+    // No CTA leaves while its partial sums may still be read. The barrier is
+    // relaxed; see cluster_leave for why that is enough here.
+    cluster_leave();
   }
 }
 

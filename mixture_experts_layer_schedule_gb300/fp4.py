@@ -182,7 +182,9 @@ class FP4Linear:
 class FP4GatedFFN:
     """The gated feed-forward block of GatedFFN with 4-bit weights, for serving:
     the gated product, then the down product, each quantising its input in the
-    call. Two launches for up to 32 tokens.
+    call. Two launches for few tokens (up to 32 at 4096 x 1536); with more tokens, or
+    wider or deeper weights, a product's input is quantised by a launch of its own where
+    that is expected to be faster.
 
     x_scale and act_scale are the NVFP4 tensor scales of x and of the inner
     activations. At 1 a block of 16 values whose largest magnitude is at most
